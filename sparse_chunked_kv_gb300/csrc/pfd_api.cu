@@ -597,7 +597,9 @@ pfd_status decode_impl(const pfd_bf16* q, const pfd_bf16* k_self, const pfd_bf16
   if (qp.staged) {
     sw = stage_ws_layout(ws.total, total_sel, max_chunk_len, Hkv, D);   // (rows < 8 GB / 256 bytes)
   }
-  if (workspace_bytes < std::max(ws.total, sw.total) || (ws.total > 0 && workspace == nullptr) ||
+  // (A staged step of one split has no partial outputs, but its chunks' copies.)
+  const size_t need = std::max(ws.total, sw.total);
+  if (workspace_bytes < need || (need > 0 && workspace == nullptr) ||
       (reinterpret_cast<uintptr_t>(workspace) & 255u) != 0)
     return PFD_ERR_INVALID_ARG;
   const float scale = sm_scale > 0.0f ? sm_scale : 1.0f / std::sqrt(static_cast<float>(D));

@@ -100,6 +100,27 @@ def test_decode_partial_host_checks(lib, over, status):
     assert _call(lib, "pfd_decode_partial_quant", args, over) == status
 
 
+STAGED = dict(lq=_host(0, 400, 800), ks=_host(0, 8, 16), Hq=28, Hkv=4, D=128, longest=2049,
+              rows=4096, bytes=1 << 40)
+
+
+@pytest.mark.parametrize("splits", [1, 2])
+@pytest.mark.parametrize("partial", [False, True])
+def test_a_staged_step_needs_its_workspace(lib, partial, splits):
+    """Many rows: the chunks are read back to the workspace, with one split too,
+    where no partial outputs need one."""
+    args = dict(DECODE, **STAGED, splits=splits)
+    need = _abi.pfd_decode_quant_workspace(2, [0, 400, 800], [0, 8, 16], 28, 4, 128, 2049, 1, splits)
+    assert need >= 16 * 2049 * 4 * 4 * 128
+    if partial:
+        items = list(args.items())
+        at = [k for k, _ in items].index("splits")
+        args = dict(items[:at] + [("self_keys", 1)] + items[at:])
+    name = "pfd_decode_partial_quant" if partial else "pfd_decode_attention_quant"
+    for over in (dict(p_ws=0), dict(bytes=need - 1), dict(p_ws=128)):
+        assert _call(lib, name, args, over) == INVALID, over
+
+
 @pytest.mark.parametrize("over,status", [
     (dict(p_q=0), INVALID), (dict(p_pk=0), INVALID), (dict(p_ek=0), INVALID), (dict(p_lse=0), INVALID),
     (dict(p_mass=0), INVALID), (dict(fmt=2), INVALID), (dict(rows=40), INVALID),
