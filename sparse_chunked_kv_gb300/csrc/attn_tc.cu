@@ -1208,7 +1208,9 @@ attention_kernel(const __grid_constant__ AttnParams p) {
                 m_used = m_new;
               }
             }
-            const float neg_m = -m_used;
+            // (A row whose logits so far are all -inf has no reference yet: with 0 their
+            // probabilities are 0, where -inf - -inf would be NaN.)
+            const float neg_m = !kMassMode && m_used == -INFINITY ? 0.0f : -m_used;
             const uint64_t scale2 = f2_pack(scale, scale), neg_m2 = f2_pack(neg_m, neg_m);
             uint64_t sum2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
             uint64_t gsum2[4] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f), f2_pack(0.f, 0.f),

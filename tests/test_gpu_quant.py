@@ -473,6 +473,75 @@ def test_decode_non_finite_live_rows(lq, more):
         st.check(out, lse, clean)
 
 
+MINUS_INF = {
+    # live rows, chunks, and a number of splits that leaves one with live keys alone
+    "rows": (5, [[64, 128]], 13),
+    "tile": (30, [[64, 128]], 14),
+    "tiles": (40, [[64, 128]], 15),
+    "staged": (320, [[2049] * 8], 64),
+}
+
+
+def _at_minus_inf(st, keys):
+    """Gives these live keys (a slice) logits of -inf from every query."""
+    st.q[:, :, 7] = st.q[:, :, 7].abs() + 0.5
+    st.k_self[keys, :, 7] = -math.inf
+
+
+@pytest.mark.parametrize("name", sorted(MINUS_INF))
+def test_split_with_logits_of_minus_infinity_only(name):
+    """Live keys at logit -inf count for nothing, also where a split holds no
+    others, by each of the ways a step may run and over the bf16 pool."""
+    lq, chunk_lens, n_splits = MINUS_INF[name]
+    st = Step("e4m3", 8, 2, 64, [lq], chunk_lens, seed=40)
+    _at_minus_inf(st, slice(None))
+    host = st.table.cpu().numpy()
+    keys, vals = (R.keys_of(values_of(st.pool, x), host, st.sel_host) for x in "kv")
+    ref = R.decode(f64(st.q), keys, vals, 1 / 8)
+    k, v, table = api.pool_dequantize(st.pool, st.table, st.table[:, 0].contiguous(), st.pool.rows)
+    # The bf16 pool's splits keep their outputs in bf16: half a step of each, so of
+    # their weighed sum, 2^-8 A at most; the bound without it is 2^-8 A at least.
+    ref2 = (ref[0], ref[1], 2 * ref[2], ref[3])
+    for n in (0, 1, n_splits):
+        st.check(*st.run(n), ref)
+        out, lse = api.decode_attention(P.cuda(st.q), P.cuda(st.k_self), P.cuda(st.v_self), k, v,
+                                        table, st.sel, n_splits=n)
+        st.check(out, lse, ref2)
+
+
+@pytest.mark.parametrize("lq", [3, 20, 32, 40, 200])
+@pytest.mark.parametrize("first", [16, 64, 128, 200])
+def test_first_logits_of_minus_infinity(lq, first):
+    """The first keys of a row at logit -inf, up to all of them: the others
+    decide, and a row with no other gives 0 and -inf."""
+    st = Step("e4m3", 8, 2, 64, [lq], [[]], seed=41)
+    cut = min(first, lq)
+    _at_minus_inf(st, slice(0, cut))
+    ref = R.decode(f64(st.q), f64(st.k_self[cut:]), f64(st.v_self[cut:]), 1 / 8)
+    ref2 = (ref[0], ref[1], 2 * ref[2], ref[3])
+    for n in (1, 2, 64):
+        st.check(*st.run(n), ref)
+        out, lse = api.decode_attention(P.cuda(st.q), P.cuda(st.k_self), P.cuda(st.v_self), st.pool.k[:0].bfloat16(),
+                                        st.pool.v[:0].bfloat16(), st.table[:0], st.sel, n_splits=n)
+        st.check(out, lse, ref2)
+
+
+def test_nan_shows_through_bf16_splits():
+    """The bf16 pool's calls: a split whose keys are all NaN, and a NaN among a
+    split's others, reach their head's rows and no others'."""
+    st = Step("e4m3", 8, 2, 64, [40], [[256] * 4], seed=8)
+    k, v, table = api.pool_dequantize(st.pool, st.table, st.table[:, 0].contiguous(), st.pool.rows)
+    row = st.table.cpu().tolist()[st.sel_host[1]][0]
+    for rows in (slice(row, row + 256), slice(row + 9, row + 10)):
+        bad = k.clone()
+        bad[rows, 1] = math.nan
+        for n in (1, 4, 8):
+            out, lse = api.decode_attention(P.cuda(st.q), P.cuda(st.k_self), P.cuda(st.v_self), bad, v,
+                                            table, st.sel, n_splits=n)
+            assert torch.isnan(out[:, 4:]).all() and torch.isnan(lse[:, 4:]).all()
+            assert torch.isfinite(out[:, :4]).all() and torch.isfinite(lse[:, :4]).all()
+
+
 def test_steps_without_rows_or_chunks():
     """Nothing to compute: outputs of no rows, a mass of zeros, an empty mass."""
     st = Step("int8", 8, 2, 64, [3], [[64, 17]], seed=16)
