@@ -78,6 +78,9 @@ constexpr int kQLoaderWarp = 10;
 constexpr int kWgThreads = 128;
 constexpr int kRing = 4;                         // tile metadata slots
 constexpr float kRescaleThreshold = 8.0f;        // log2 units
+constexpr float kNoRef = -3.402823466e38f;       // reference of a row that has seen no logit but -inf:
+                                                 // finite, so that such a logit's probability is
+                                                 // 0 (from -inf it would be NaN)
 constexpr uint32_t kPanelBytes = 128u * 128u;    // 128 rows x 128 B
 constexpr uint32_t kTmemCols = 512;
 constexpr float kLn2 = 0.69314718055994530942f;
@@ -1029,7 +1032,7 @@ attention_kernel(const __grid_constant__ AttnParams p) {
       if (!resolve_item<kPrefill, kMassMode, kSeqItems>(p, idx, it)) continue;
       const bool with_pv = it.kind != kWindow && it.kind != kMass;
       const bool active = x == 0 || it.has_b;
-      float m_used = -INFINITY, l_sum = 0.0f;
+      float m_used = kNoRef, l_sum = 0.0f;
       // Chunk-mass items: this row's probability mass in each of the item's
       // chunks (segments), accumulated group by group.
       float seg_mass[kMassChunks];
@@ -1208,9 +1211,7 @@ attention_kernel(const __grid_constant__ AttnParams p) {
                 m_used = m_new;
               }
             }
-            // (A row whose logits so far are all -inf has no reference yet: with 0 their
-            // probabilities are 0, where -inf - -inf would be NaN.)
-            const float neg_m = !kMassMode && m_used == -INFINITY ? 0.0f : -m_used;
+            const float neg_m = -m_used;
             const uint64_t scale2 = f2_pack(scale, scale), neg_m2 = f2_pack(neg_m, neg_m);
             uint64_t sum2[2] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f)};
             uint64_t gsum2[4] = {f2_pack(0.f, 0.f), f2_pack(0.f, 0.f), f2_pack(0.f, 0.f),
