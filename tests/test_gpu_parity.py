@@ -8,6 +8,7 @@ from oracle import pfd_oracle as orc
 from sparse_chunked_kv_gb300 import _abi, api
 from sparse_chunked_kv_gb300 import workloads as wl
 from tests import parity as P
+from tests import quant_reference as R
 
 pytestmark = pytest.mark.gpu
 
@@ -520,3 +521,40 @@ def test_decode_bf16_partials_error_margin(capsys):
         lines.append(f"S={s} vs S=1: out max {d.max():.3e} mean {d.mean():.3e}")
     with capsys.disabled():
         print("\n" + "\n".join(lines))
+
+
+@pytest.mark.parametrize("with_self", [False, True])
+def test_prefill_keys_at_minus_infinity(with_self):
+    """Keys at logit -inf from every query take no weight: the first 70 rows of a
+    chunk, its BOS row, and every row of one (whose outputs and scores are 0)."""
+    n, c, w, hq, hkv, d, keep = 3, 200, 8, 8, 2, 64, 16
+    g = torch.Generator().manual_seed(50)
+    q, k, v = (torch.randn(n * (c + 1), h, d, generator=g).to(torch.bfloat16) for h in (hq, hkv, hkv))
+    q_win, k_win = (torch.randn(w, h, d, generator=g).to(torch.bfloat16) for h in (hq, hkv))
+    q[:, :, 7], q_win[:, :, 7] = q[:, :, 7].abs() + 0.5, q_win[:, :, 7].abs() + 0.5
+    out_of = torch.zeros(n, c + 1, dtype=torch.bool)
+    out_of[0, 1:71], out_of[1, 0], out_of[2] = True, True, True
+    k[out_of.reshape(-1), :, 7] = float("-inf")
+    slot = torch.arange(n, dtype=torch.int32, device="cuda") * (keep + 1)
+    res = api.chunk_prefill_ex(P.cuda(q), P.cuda(k), P.cuda(v), P.cuda(q_win),
+                               P.cuda(k_win) if with_self else None, n, c, keep, slot, n * (keep + 1))
+    torch.cuda.synchronize()
+    assert int(res["dev_err"].item()) == 0
+    scores = res["scores"].cpu().double().numpy().reshape(n, c + 1)
+    out = res["out"].cpu().double().numpy().reshape(n, c + 1, hq, d)
+    for j in range(n):
+        rows = slice(j * (c + 1), (j + 1) * (c + 1))
+        seen = ~out_of[j].numpy()
+        keys, vals = f64(k[rows])[seen], f64(v[rows])[seen]
+        want, _, tol, _ = R.decode(f64(q[rows]), keys, vals, d ** -0.5)
+        assert (np.abs(out[j] - want) <= tol).all()
+        ref = np.zeros(c + 1)
+        for h in range(hq):
+            kv = h * hkv // hq
+            s = f64(q_win[:, h]) @ keys[:, kv].T * d ** -0.5
+            own = f64(q_win[:, h]) @ f64(k_win[:, kv]).T * d ** -0.5
+            both = np.concatenate([s, own], axis=1) if with_self else s
+            if both.shape[1] > 0:
+                top = both.max(axis=1, keepdims=True)
+                ref[seen] += (np.exp(s - top) / np.exp(both - top).sum(axis=1, keepdims=True)).sum(axis=0)
+        assert (np.abs(scores[j] - ref) <= P.score_tol(ref, w, hq)).all()
