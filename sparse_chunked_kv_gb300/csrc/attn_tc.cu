@@ -1295,7 +1295,9 @@ attention_kernel(const __grid_constant__ AttnParams p) {
         // mass-sum kernel.
         const int t_local = row / G;
         const int t = (it.ta + x) * p.Tq + t_local;
-        const bool row_in = active && row < q_rows && t < it.n_t;
+        // (Without a finite lse a row's reference is +inf, which makes finite logits add 0;
+        // a NaN or infinity in the query, the usual cause, has other logits.)
+        const bool row_in = active && row < q_rows && t < it.n_t && m_used != INFINITY;
         if constexpr (kMassMulti) {
           const int nchunks = it.k1 - it.k0;
 #pragma unroll

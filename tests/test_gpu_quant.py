@@ -583,6 +583,35 @@ def test_mass_without_a_finite_normaliser():
     assert (np.abs(got - want) <= tol).all()
 
 
+@pytest.mark.parametrize("bad", [math.nan, math.inf, -math.inf])
+@pytest.mark.parametrize("lens", [[100, 31, 16], [17] * 1100])   # one chunk an item, and several
+@pytest.mark.parametrize("lq", [5, 40])
+def test_mass_of_a_query_row_that_is_not_finite(lq, lens, bad):
+    """A NaN or an infinity in a query row makes its lse NaN; the row adds nothing
+    to any chunk, over the 8-bit and the bf16 pool, and the others what they did."""
+    st = Step("e4m3", 8, 2, 64, [lq], [lens], seed=17, spare=0)
+    st.cu_k, st.sel = [0, 3], st.sel[:3].clone()      # the step selects three chunks
+    n = st.table.shape[0]
+    st.q[1, 3, 9], st.q[lq - 1, 6, 0] = bad, bad
+    q = P.cuda(st.q)
+    _, lse = st.run()
+    hit = torch.zeros(lq, 8, dtype=torch.bool)
+    hit[1, 3] = hit[lq - 1, 6] = True
+    assert torch.equal(torch.isnan(lse).cpu(), hit)
+    got = api.chunk_mass_quant(q, st.pool, st.table, lse, api.QuantMassPlan([0, lq], [0, n], 8, 2, 64))
+    k, _, table = api.pool_dequantize(st.pool, st.table, st.table[:, 0].contiguous(), st.pool.rows)
+    mass = torch.full((n,), 7.0, device="cuda")
+    need = _abi.pfd_chunk_mass_workspace(1, [0, lq], [0, n], 8, 2)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    _abi.pfd_chunk_mass(q, ints([0, lq]), [0, lq], k, k.shape[0], table, n, [0, n], lse, 1, 8, 2, 64,
+                        0.0, mass, None, ws, need)
+    x, at = f64(st.q), f64(lse.cpu())
+    x[hit.numpy()], at[hit.numpy()] = 0.0, 1e4        # exp(0 - 1e4) = 0
+    want, tol = R.mass(x, values_of(st.pool, "k"), st.table.cpu().numpy(), range(n), at, 1 / 8)
+    for m in (got, mass):
+        assert (np.abs(m.cpu().to(torch.float64).numpy() - want) <= tol).all()
+
+
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("case", ["small", "batch", "many", "one"])
 def test_mass_matches_the_reference(case, fmt):
