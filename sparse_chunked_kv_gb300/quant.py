@@ -233,22 +233,25 @@ def pool_dequantize(pool, table, dst_row, dst_rows=None, sel=None, max_len=None,
                     dst_table=None, dev_err=None, stream=None):
     """Reads slots of an 8-bit pool back as bf16 (pfd_pool_dequantize): the
     rows of table[sel[j]] (sel None: table[j]) go to rows dst_row[j] .. of k, v
-    [dst_rows, Hkv, D].  Rows that no slot covers are left as they were, or
-    undefined where k and v are allocated here.  Returns (k, v, dst_table)."""
+    [dst_rows, Hkv, D], at least one row where there are slots.  Rows that no slot
+    covers are left as they were, or undefined where k and v are allocated here.
+    Returns (k, v, dst_table)."""
     dev, hkv, d = pool.device, pool.n_kv_heads, pool.head_dim
     table_len = _rows(table, "table")
     n = table_len if sel is None else _rows(sel, "sel")
+    if (k is None) != (v is None) or (k is None and dst_rows is None):
+        raise ValueError("expected k and v, or dst_rows")
+    rows = _rows(k, "k") if dst_rows is None else dst_rows
+    if rows < (1 if n > 0 else 0):
+        raise ValueError(f"dst_rows: expected rows for {n} slots, got {rows}")
     _need(table, _I32, (table_len, 2), "table", dev)
     if sel is not None:
         _need(sel, _I32, (n,), "sel", dev)
     _need(dst_row, _I32, (n,), "dst_row", dev)
-    if (k is None) != (v is None) or (k is None and dst_rows is None):
-        raise ValueError("expected k and v, or dst_rows")
     err = _error_word(dev_err, dev)
     if k is not None:
-        shape = (_rows(k, "k") if dst_rows is None else dst_rows, hkv, d)
-        _need(k, _BF16, shape, "k", dev)
-        _need(v, _BF16, shape, "v", dev)
+        _need(k, _BF16, (rows, hkv, d), "k", dev)
+        _need(v, _BF16, (rows, hkv, d), "v", dev)
     if dst_table is not None:
         _need(dst_table, _I32, (n, 2), "dst_table", dev)
         if dst_table.data_ptr() == table.data_ptr() and n > 0:
@@ -257,12 +260,11 @@ def pool_dequantize(pool, table, dst_row, dst_rows=None, sel=None, max_len=None,
     def body():
         to_k, to_v, to_table = k, v, dst_table
         if to_k is None:
-            to_k = torch.empty((dst_rows, hkv, d), dtype=_BF16, device=dev)
+            to_k = torch.empty((rows, hkv, d), dtype=_BF16, device=dev)
             to_v = torch.empty_like(to_k)
         if to_table is None:
             to_table = torch.empty((n, 2), dtype=_I32, device=dev)
-        rows = to_k.shape[0]
-        if n > 0 and rows > 0:
+        if n > 0:
             _abi._check(_abi.load().pfd_pool_dequantize(
                 *pool.pointers, pool.rows, table.data_ptr(), table_len,
                 None if sel is None else sel.data_ptr(), n, _longest(table, max_len), hkv, d,

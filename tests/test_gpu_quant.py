@@ -170,6 +170,24 @@ def test_slot_errors_are_reported_and_skipped():
     assert read([48, 16], 0, 48) == (0, [48, 16], False)
 
 
+def test_reading_back_into_no_rows():
+    """Slots without a destination row are refused, empty ones too; no slots need
+    none, and empty slots with a row get their entries."""
+    pool = api.QuantPool.zeros(64, 2, 64)
+    for entry in ([0, 0], [0, 5]):
+        with pytest.raises(ValueError, match="dst_rows"):
+            api.pool_dequantize(pool, ints([entry]), ints([0]), 0)
+    none = torch.empty(0, 2, 64, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(ValueError, match="dst_rows"):
+        api.pool_dequantize(pool, ints([[0, 0]]), ints([0]), k=none, v=none)
+    k, v, table = api.pool_dequantize(pool, torch.empty(0, 2, dtype=torch.int32, device="cuda"),
+                                      torch.empty(0, dtype=torch.int32, device="cuda"), 0)
+    assert k.shape == v.shape == (0, 2, 64) and table.shape == (0, 2)
+    given, err = ints([[7, 7], [7, 7], [7, 7]]), ints([0])
+    api.pool_dequantize(pool, ints([[0, 0], [16, 0], [32, 2]]), ints([0, 1, 1]), 1, dst_table=given, dev_err=err)
+    assert given.tolist() == [[0, 0], [1, 0], [0, 0]] and int(err.item()) == _abi.DEVERR_SLOT
+
+
 # ---------------------------------------------------------------- decode --
 
 class Step:

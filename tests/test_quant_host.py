@@ -222,6 +222,15 @@ def test_a_partial_plan_is_not_a_whole_step():
         api.decode_attention_quant(None, None, None, _Pool, None, None, plan)
 
 
+@pytest.mark.parametrize("rows", [dict(dst_rows=0), dict(dst_rows=-1),
+                                  dict(k=_bf(0, 2, 64), v=_bf(0, 2, 64))])
+def test_reading_slots_back_needs_rows(rows, monkeypatch):
+    """Without a destination row nothing would say where the slots are."""
+    _no_library(monkeypatch)
+    with pytest.raises(ValueError, match="dst_rows"):
+        api.pool_dequantize(_Pool, _i32(1, 2), _i32(1), max_len=8, **rows)
+
+
 def test_api_offers_the_module():
     for name in ("QuantPool", "QuantDecodePlan", "QuantMassPlan", "pool_quantize", "pool_dequantize",
                  "decode_attention_quant", "decode_partial_quant", "chunk_mass_quant"):
