@@ -514,7 +514,8 @@ pfd_status pfd_decode_attention_static_scratch(
  *   pool_k/v    [pool_rows, Hkv, D] codes, 16-byte aligned (written)
  *   exp_k/v     [pool_rows / 16, Hkv] exponent bytes (written)
  *   slot_row    [n_slots] int32, multiples of 16; overlap is not checked
- *   table       [n_slots] pfd_chunk_entry (written; not src_table itself)
+ *   table       [n_slots] pfd_chunk_entry (written; shares no memory with
+ *               src_table or slot_row)
  * A source entry outside the rows sets PFD_DEVERR_TABLE, a slot that is
  * misplaced or does not fit sets PFD_DEVERR_SLOT; that slot is not written and
  * its entry is {0, 0}.  HBM-bound: 2 bytes read and 1 written per element.
@@ -534,6 +535,8 @@ pfd_status pfd_pool_quantize(const pfd_bf16* k, const pfd_bf16* v, int64_t src_r
  *              overlap is not checked
  *   sel        [n_slots] int32 indices into table, or NULL (n_slots <= table_len)
  *   max_len    upper bound of table[].len, used only to plan the launch
+ *   dst_table  [n_slots] pfd_chunk_entry (written; shares no memory with table,
+ *              sel or dst_row)
  * Device-side errors: PFD_DEVERR_SEL, PFD_DEVERR_TABLE, PFD_DEVERR_SLOT (the
  * rows do not fit dst_rows); that slot's rows are not written and its
  * dst_table entry is {0, 0}.

@@ -1109,6 +1109,13 @@ pfd_status quant_rows_status(const void* k, const void* v, int64_t rows, const v
   return PFD_OK;
 }
 
+// A slot's CTAs read its entries while one of them writes its new one, so the
+// written table may share no byte with what is read through the slots' numbers.
+bool shares_bytes(const void* a, size_t a_bytes, const void* b, size_t b_bytes) {
+  const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+  return a != nullptr && b != nullptr && x < y + b_bytes && y < x + a_bytes;
+}
+
 // CTAs per slot: one warp per (16-row block, K or V, head) of a slot of
 // max_len rows; longer slots are walked with that stride.
 bool plan_quant(QuantParams* p, int max_len, int64_t rows, int64_t pool_rows) {
@@ -1188,6 +1195,10 @@ pfd_status pfd_pool_quantize(const pfd_bf16* k, const pfd_bf16* v, int64_t src_r
   p.Hkv = Hkv;
   p.D = D;
   if (!plan_quant(&p, max_len, src_rows, pool_rows)) return PFD_ERR_UNSUPPORTED;
+  const size_t slots = static_cast<size_t>(n_slots);
+  if (shares_bytes(table, slots * sizeof(*table), src_table, slots * sizeof(*src_table)) ||
+      shares_bytes(table, slots * sizeof(*table), slot_row, slots * sizeof(*slot_row)))
+    return PFD_ERR_INVALID_ARG;
   return from_cuda(launch_pool_quantize(p, format + 1, reinterpret_cast<cudaStream_t>(stream)));
 }
 
@@ -1222,6 +1233,12 @@ pfd_status pfd_pool_dequantize(const uint8_t* pool_k, const uint8_t* pool_v, con
   p.Hkv = Hkv;
   p.D = D;
   if (!plan_quant(&p, max_len, dst_rows, pool_rows)) return PFD_ERR_UNSUPPORTED;
+  const size_t slots = static_cast<size_t>(n_slots);
+  if (shares_bytes(dst_table, slots * sizeof(*dst_table), table,
+                   static_cast<size_t>(table_len) * sizeof(*table)) ||
+      shares_bytes(dst_table, slots * sizeof(*dst_table), sel, slots * sizeof(*sel)) ||
+      shares_bytes(dst_table, slots * sizeof(*dst_table), dst_row, slots * sizeof(*dst_row)))
+    return PFD_ERR_INVALID_ARG;
   return from_cuda(launch_pool_dequantize(p, format + 1, reinterpret_cast<cudaStream_t>(stream)));
 }
 

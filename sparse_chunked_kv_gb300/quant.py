@@ -51,6 +51,17 @@ def _rows(tensor, what):
     return tensor.shape[0]
 
 
+def _apart(written, what, **read):
+    """The entries that a call writes share no memory with those it reads."""
+    if written is None:
+        return
+    start = written.data_ptr()
+    end = start + written.numel() * written.element_size()
+    for name, t in read.items():
+        if t is not None and start < t.data_ptr() + t.numel() * t.element_size() and t.data_ptr() < end:
+            raise ValueError(f"{what}: may not share memory with {name}")
+
+
 def _error_word(dev_err, device):
     if dev_err is None:
         return None
@@ -214,8 +225,7 @@ def pool_quantize(k, v, src_table, pool, slot_row, max_len=None, table=None, dev
     err = _error_word(dev_err, dev)
     if table is not None:
         _need(table, _I32, (n, 2), "table", dev)
-        if table.data_ptr() == src_table.data_ptr() and n > 0:
-            raise ValueError("table: may not be src_table itself")
+        _apart(table, "table", src_table=src_table, slot_row=slot_row)
 
     def body():
         out = torch.empty_like(src_table) if table is None else table
@@ -254,8 +264,7 @@ def pool_dequantize(pool, table, dst_row, dst_rows=None, sel=None, max_len=None,
         _need(v, _BF16, (rows, hkv, d), "v", dev)
     if dst_table is not None:
         _need(dst_table, _I32, (n, 2), "dst_table", dev)
-        if dst_table.data_ptr() == table.data_ptr() and n > 0:
-            raise ValueError("dst_table: may not be table itself")
+        _apart(dst_table, "dst_table", table=table, sel=sel, dst_row=dst_row)
 
     def body():
         to_k, to_v, to_table = k, v, dst_table

@@ -61,6 +61,35 @@ def test_dequantize_host_checks(lib, over, status):
     assert _call(lib, "pfd_pool_dequantize", DEQUANTIZE, over) == status
 
 
+@pytest.mark.parametrize("name,args,written,read", [
+    ("pfd_pool_quantize", QUANTIZE, "p_table", ("p_src", "p_slot")),
+    ("pfd_pool_dequantize", DEQUANTIZE, "p_dt", ("p_table", "p_sel", "p_dst"))])
+def test_the_written_table_is_apart_from_what_is_read(lib, name, args, written, read):
+    """Two entries of 8 bytes that begin before, at and inside the other's."""
+    for other in read:
+        for at in (1008, 1016, 1020):
+            over = {written: 1016, other: at}
+            if at == 1008 and other not in ("p_src", "p_table"):
+                over[other] = 1012            # (two of 4 bytes)
+            assert _call(lib, name, args, over) == INVALID, (other, at)
+
+
+def test_shared_entries_are_refused(monkeypatch):
+    monkeypatch.setattr(quant, "_need", lambda *a: None)
+    _no_library(monkeypatch)
+    t = _i32(8, 2)
+    with pytest.raises(ValueError, match="src_table"):
+        api.pool_quantize(_bf(8, 2, 64), _bf(8, 2, 64), t[:3], _Pool, _i32(3), max_len=8, table=t[2:5])
+    with pytest.raises(ValueError, match="slot_row"):
+        api.pool_quantize(_bf(8, 2, 64), _bf(8, 2, 64), t[:3], _Pool, t[4:6].view(-1)[:3], max_len=8,
+                          table=t[3:6])
+    for name, kw in (("table", dict(dst_table=t[7:8])), ("sel", dict(dst_table=_i32(1, 2)))):
+        if name == "sel":
+            kw["sel"] = kw["dst_table"].view(-1)[1:]
+        with pytest.raises(ValueError, match=name):
+            api.pool_dequantize(_Pool, t, _i32(1), 8, max_len=8, **dict(dict(sel=_i32(1)), **kw))
+
+
 def _host(*values):
     return ctypes.cast((ctypes.c_int32 * len(values))(*values), ctypes.c_void_p)
 
