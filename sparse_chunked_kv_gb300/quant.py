@@ -84,8 +84,11 @@ def _switched(device, stream):
 
 def _call(device, stream, body):
     """Runs body() with the call's device and stream the current ones."""
-    if stream is None and device.index == torch.cuda.current_device():
-        return body()
+    if stream is None:
+        if device.index == torch.cuda.current_device():
+            return body()
+    elif not isinstance(stream, int) and stream.device != device:
+        raise ValueError(f"stream: on {stream.device}, the call on {device}")
     with _switched(device, stream):
         return body()
 

@@ -260,6 +260,22 @@ def test_reading_slots_back_needs_rows(rows, monkeypatch):
         api.pool_dequantize(_Pool, _i32(1, 2), _i32(1), max_len=8, **rows)
 
 
+def test_a_stream_of_another_device_is_refused(monkeypatch):
+    """Its device would become the current one, with every pointer on the pool's."""
+    monkeypatch.setattr(quant, "_need", lambda *a: None)
+    _no_library(monkeypatch)
+    other = type("Stream", (), dict(device=torch.device("cuda", 1)))()
+    for call in (
+            lambda: api.pool_quantize(_bf(8, 2, 64), _bf(8, 2, 64), _i32(1, 2), _Pool, _i32(1),
+                                      max_len=8, stream=other),
+            lambda: api.pool_dequantize(_Pool, _i32(1, 2), _i32(1), 8, max_len=8, stream=other),
+            lambda: api.decode_partial_quant(_bf(3, 4, 64), None, None, _Pool, _i32(1, 2), _i32(1),
+                                             type("P", (_Plan,), dict(self_keys=False, given_workspace=lambda s, w: w))(),
+                                             stream=other)):
+        with pytest.raises(ValueError, match="stream"):
+            call()
+
+
 def test_api_offers_the_module():
     for name in ("QuantPool", "QuantDecodePlan", "QuantMassPlan", "pool_quantize", "pool_dequantize",
                  "decode_attention_quant", "decode_partial_quant", "chunk_mass_quant"):
