@@ -484,8 +484,9 @@ pfd_status pfd_decode_attention_static_scratch(
  * block).  A table entry at another row counts as out of range
  * (PFD_DEVERR_TABLE).
  * The scale is a power of two so that a value is exact in bf16 (8 significant
- * bits at most): attention over the codes has the logits and values of
- * attention over the dequantised bf16 rows.
+ * bits at most; E4M3 from byte 3 on, where its smallest codes are still bf16
+ * numbers, and pfd_pool_quantize writes none below 27): attention over the codes
+ * has the logits and values of attention over the dequantised bf16 rows.
  */
 #define PFD_KV_BLOCK 16 /* rows that share a scale */
 #define PFD_KV_E4M3 0   /* format: 4 exponent, 3 mantissa bits, |code| <= 448 */

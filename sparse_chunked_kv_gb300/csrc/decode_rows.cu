@@ -486,7 +486,9 @@ decode_rows_kernel(const __grid_constant__ RowsParams p) {
       const uint32_t ek = (info >> 8) & 0xFFu, e = info >> 16;
       const float nan = __uint_as_float(0x7FC00000u);
       nv[g] = static_cast<int>(info & 0xFFu);
-      ks[g] = ek == 255u ? nan : two_to(static_cast<int>(ek) - 127);
+      // 2^(ek - 127): the byte as an exponent, with the mantissa's upper bit for byte 0
+      // (2^-127 is subnormal) and for byte 255 (a NaN)
+      ks[g] = __uint_as_float((ek << 23) | (((ek + 1u) & 0xFEu) == 0u ? 0x00400000u : 0u));
       ev[g] = e == 255u ? nan : static_cast<float>(static_cast<int>(e) - 127);
     }
     float s[2][NT][4] = {};
@@ -663,8 +665,14 @@ decode_rows_kernel(const __grid_constant__ RowsParams p) {
       o.z = fmaf(x.z, f, o.z);
       o.w = fmaf(x.w, f, o.w);
     }
-    // O is relative to 2^(y - 7), l to 2^m
-    const float f = l == 0.0f ? 0.0f : ex2_approx(y - kProbBias - m) / l;   // (l is NaN where a logit was)
+    // O is relative to 2^(y - 7), l to 2^m.  (l is NaN where a logit was.)
+    float e = y - kProbBias - m;
+    if (e < -60.0f) {   // V scales near 2^-127: ex2_approx gives 0 below 2^-126, so two factors
+      const float down = two_to(-64);
+      o = make_float4(o.x * down, o.y * down, o.z * down, o.w * down);
+      e += 64.0f;
+    }
+    const float f = l == 0.0f ? 0.0f : ex2_approx(e) / l;
     const int t = row / p.G, j = row - t * p.G;
     const long long at = static_cast<long long>(lq0 + t) * p.Hq + head * p.G + j;
     if (whole) {

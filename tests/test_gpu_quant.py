@@ -344,6 +344,46 @@ def test_decode_scales_far_from_one(fmt, lq):
     st.check(*st.run())
 
 
+@pytest.mark.parametrize("lq,more", [(1, 0), (20, 0), (40, 0), (200, 8)])
+@pytest.mark.parametrize("fmt,byte", [("int8", 0), ("int8", 1), ("int8", 9), ("e4m3", 3), ("e4m3", 9)])
+def test_scales_at_the_low_end(fmt, byte, lq, more):
+    """Scales down to 2^-127, smaller than any that quantising writes, by each of the
+    ways a step may run and in a mass: every value is exact in bf16 down to
+    2^-133 (E4M3 codes are multiples of 2^-9, so from byte 3 on)."""
+    st = Step(fmt, 8, 2, 64, [lq], [[64, 40] + [2049] * more], seed=42, self_keys=False, spare=0)
+    st.pool.exp_v.fill_(byte)
+    ref = st.reference()
+    for n_splits in (1, 3):
+        st.check(*st.run(n_splits), ref)
+    st.pool.exp_v.fill_(127)
+    st.pool.exp_k.fill_(byte)
+    st.q = (st.q.float() * 2.0 ** (120 - byte)).to(torch.bfloat16)   # the logits of scale 2^-7
+    ref = st.reference()
+    for n_splits in (1, 3):
+        out, lse = st.run(n_splits)
+        st.check(out, lse, ref)
+    n = st.table.shape[0]
+    got = api.chunk_mass_quant(P.cuda(st.q), st.pool, st.table, lse,
+                               api.QuantMassPlan([0, lq], [0, n], 8, 2, 64))
+    want, tol = R.mass(f64(st.q), values_of(st.pool, "k"), st.table.cpu().numpy(), range(n),
+                       f64(lse.cpu()), 1 / 8)
+    assert (np.abs(got.cpu().to(torch.float64).numpy() - want) <= tol).all()
+
+
+@pytest.mark.parametrize("byte", [0, 1, 2])
+def test_scales_at_the_low_end_few_rows(byte):
+    """The few-rows kernel takes codes in f16 and scales in fp32: exact from byte 0 on."""
+    st = Step("e4m3", 8, 2, 64, [3], [[64, 40]], seed=43, self_keys=False, spare=0)
+    st.pool.exp_v.fill_(byte)
+    for n_splits in (1, 3):
+        st.check(*st.run(n_splits))
+    st.pool.exp_v.fill_(127)
+    st.pool.exp_k.fill_(byte)
+    st.q = (st.q.float() * 2.0 ** (120 - byte)).to(torch.bfloat16)
+    for n_splits in (1, 3):
+        st.check(*st.run(n_splits))
+
+
 @pytest.mark.parametrize("fmt", FORMATS)
 @pytest.mark.parametrize("d", [64, 128])
 @pytest.mark.parametrize("lq", [40, 320])
