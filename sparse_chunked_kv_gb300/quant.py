@@ -101,7 +101,8 @@ def _raw_stream(device):
 
 class QuantPool:
     """An 8-bit chunk pool: codes k, v [pool_rows, Hkv, D] and exponent bytes
-    exp_k, exp_v [pool_rows / 16, Hkv] (torch.uint8)."""
+    exp_k, exp_v [pool_rows / 16, Hkv] (torch.uint8).  Their contents may be
+    changed in place; other tensors make another pool."""
 
     def __init__(self, k, v, exp_k, exp_v):
         if k.dtype not in _FORMATS:
@@ -118,10 +119,21 @@ class QuantPool:
         _need(v, k.dtype, k.shape, "pool v", k.device)
         _need(exp_k, _U8, exps, "pool exp_k", k.device)
         _need(exp_v, _U8, exps, "pool exp_v", k.device)
-        self.k, self.v, self.exp_k, self.exp_v = k, v, exp_k, exp_v
+        self._tensors = (k, v, exp_k, exp_v)
         self.rows, self.n_kv_heads, self.head_dim = rows, hkv, d
         self.device, self.format = k.device, _FORMATS[k.dtype]
-        self.pointers = (k.data_ptr(), v.data_ptr(), exp_k.data_ptr(), exp_v.data_ptr())
+
+    # Read-only: their types and shapes are checked once, when the pool is made.
+    k = property(lambda self: self._tensors[0])
+    v = property(lambda self: self._tensors[1])
+    exp_k = property(lambda self: self._tensors[2])
+    exp_v = property(lambda self: self._tensors[3])
+
+    @property
+    def pointers(self):
+        """Addresses of k, v, exp_k and exp_v now."""
+        k, v, exp_k, exp_v = self._tensors
+        return k.data_ptr(), v.data_ptr(), exp_k.data_ptr(), exp_v.data_ptr()
 
     @classmethod
     def zeros(cls, pool_rows, n_kv_heads, head_dim, dtype=torch.float8_e4m3fn, device="cuda"):
@@ -376,7 +388,7 @@ def chunk_mass_quant(q, pool, table, lse, plan, mass=None, dev_err=None, workspa
         ws = plan.workspace() if space is None else space
         cu_lq, cu_lq_host, _, cu_n_host = plan.pointers
         _abi._check(_abi.load().pfd_chunk_mass_quant(
-            q.data_ptr(), cu_lq, cu_lq_host, pool.format, pool.pointers[0], pool.pointers[2],
+            q.data_ptr(), cu_lq, cu_lq_host, pool.format, pool.k.data_ptr(), pool.exp_k.data_ptr(),
             pool.rows, table.data_ptr(), n, cu_n_host, lse.data_ptr(), plan.batch, plan.n_q_heads,
             plan.n_kv_heads, pool.head_dim, plan.sm_scale, to.data_ptr(), err,
             None if ws is None else ws.data_ptr(), plan.workspace_bytes, _raw_stream(dev)))

@@ -236,6 +236,23 @@ def test_codes_of_another_type_are_refused():
         api.QuantPool(_bf(32, 2, 64), _bf(32, 2, 64), _i32(2, 2), _i32(2, 2))
 
 
+def test_a_pool_keeps_its_tensors(monkeypatch):
+    """Others cannot take their places unchecked, and no address outlives its memory."""
+    monkeypatch.setattr(quant, "_need", lambda *a: None)
+    codes = type("Codes", (), dict(dtype=torch.int8, is_cuda=True, device=torch.device("cuda", 0),
+                                   shape=(32, 2, 64), at=1, dim=lambda s: 3,
+                                   data_ptr=lambda s: s.at))
+    parts = [codes() for _ in range(4)]
+    pool = api.QuantPool(*parts)
+    assert (pool.k, pool.v, pool.exp_k, pool.exp_v) == tuple(parts)
+    for name in ("k", "v", "exp_k", "exp_v"):
+        with pytest.raises(AttributeError):
+            setattr(pool, name, codes())
+    assert pool.pointers == (1, 1, 1, 1)
+    parts[2].at = 5
+    assert pool.pointers == (1, 1, 5, 1)
+
+
 @pytest.mark.parametrize("cu_lq,cu_k", [([0, 2, 1], [0, 1, 2]), ([0, 2], [0, 1, 2]), ([1, 2], [0, 1]),
                                         ([0], [0])])
 def test_plans_refuse_malformed_counts(cu_lq, cu_k):
