@@ -564,7 +564,9 @@ size_t pfd_decode_quant_workspace(int batch, const int32_t* cu_lq_host, const in
  * 8-bit pool; the live block stays bf16.  Arguments and results as there, the
  * pool's codes, exponents and format in the place of its rows; a split's
  * partial output is kept in fp32.  max_chunk_len bounds the selected chunks'
- * lengths: a longer one counts as out of range (PFD_DEVERR_TABLE).
+ * lengths: a longer one counts as out of range (PFD_DEVERR_TABLE).  A sequence
+ * whose chunks may hold 2^31 blocks of 16 rows by that bound and pool_rows is
+ * PFD_ERR_UNSUPPORTED.
  * pfd_decode_partial_quant takes NULL for k_self and v_self when self_keys ==
  * 0.
  */

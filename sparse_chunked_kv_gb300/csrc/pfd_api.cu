@@ -592,6 +592,13 @@ pfd_status decode_impl(const pfd_bf16* q, const pfd_bf16* k_self, const pfd_bf16
                                              self_keys);
   const int S = qp.n_splits;
   if (pool.codes() && max_chunk_len < 0) return PFD_ERR_INVALID_ARG;
+  if (pool.codes())   // the kernels count a sequence's key groups in 31 bits
+    for (int b = 0; b < batch; ++b) {
+      const long long longest = std::min<long long>(max_chunk_len, pool_rows);
+      const long long groups = (cu_k_host[b + 1] - cu_k_host[b]) * ((longest + kGroupRows - 1) / kGroupRows) +
+                               ceil_div(cu_lq_host[b + 1] - cu_lq_host[b], kGroupRows);
+      if (groups >= (1ll << 31)) return PFD_ERR_UNSUPPORTED;
+    }
   const DecodeWs ws = decode_ws_layout(S, total_lq, Hq, D, pool.codes() ? 4 : 2);
   StageWs sw{};
   if (qp.staged) {

@@ -133,6 +133,17 @@ STAGED = dict(lq=_host(0, 400, 800), ks=_host(0, 8, 16), Hq=28, Hkv=4, D=128, lo
               rows=4096, bytes=1 << 40)
 
 
+@pytest.mark.parametrize("lq", [1, 40])
+def test_more_key_groups_than_the_kernels_count(lib, lq):
+    """One chunk may be selected many times: 17 or more of 2^31 - 16 rows are over
+    2^31 groups of 16, and a bound past the pool's rows counts as these."""
+    args = dict(DECODE, lq=_host(0, lq, lq), rows=(1 << 31) - 16, longest=2 ** 31 - 1, bytes=1 << 40)
+    assert _call(lib, "pfd_decode_attention_quant", args, dict(ks=_host(0, 17, 17))) == UNSUPPORTED
+    for over in (dict(ks=_host(0, 15, 30)), dict(ks=_host(0, 17, 17), rows=64)):
+        # (a workspace that does not start at 256 bytes ends the call at the next check)
+        assert _call(lib, "pfd_decode_attention_quant", args, dict(over, p_ws=300)) == INVALID
+
+
 @pytest.mark.parametrize("splits", [1, 2])
 @pytest.mark.parametrize("partial", [False, True])
 def test_a_staged_step_needs_its_workspace(lib, partial, splits):
