@@ -116,8 +116,8 @@ def _stream(stream):
 
 
 def _host_i32(arr):
-    """A host int32 buffer (ctypes array) from a list / CPU tensor (an array as it is)."""
-    if isinstance(arr, ctypes.Array):
+    """A host int32 buffer (ctypes array) from a list / CPU tensor (such an array as it is)."""
+    if isinstance(arr, ctypes.Array) and arr._type_ is ctypes.c_int32:
         return arr
     vals = arr.tolist() if hasattr(arr, "tolist") else list(arr)
     return (ctypes.c_int32 * len(vals))(*[int(v) for v in vals])
@@ -288,62 +288,8 @@ def pfd_reselect_chunks(s, mass, lam, cu_n, cu_k, batch, max_n, sel, s_out, stre
                                       batch, max_n, _ptr(sel), _ptr(s_out), _stream(stream)))
 
 
-def pfd_pool_quantize(k, v, src_rows, src_table, n_slots, max_len, Hkv, D, format, pool_k, pool_v,
-                      exp_k, exp_v, pool_rows, slot_row, table, dev_err, stream=None):
-    _check(load().pfd_pool_quantize(
-        _ptr(k), _ptr(v), int(src_rows), _ptr(src_table), n_slots, max_len, Hkv, D, format,
-        _ptr(pool_k), _ptr(pool_v), _ptr(exp_k), _ptr(exp_v), int(pool_rows), _ptr(slot_row),
-        _ptr(table), _ptr(dev_err), _stream(stream)))
-
-
-def pfd_pool_dequantize(pool_k, pool_v, exp_k, exp_v, pool_rows, table, table_len, sel, n_slots,
-                        max_len, Hkv, D, format, k, v, dst_rows, dst_row, dst_table, dev_err,
-                        stream=None):
-    _check(load().pfd_pool_dequantize(
-        _ptr(pool_k), _ptr(pool_v), _ptr(exp_k), _ptr(exp_v), int(pool_rows), _ptr(table),
-        int(table_len), _ptr(sel), n_slots, max_len, Hkv, D, format, _ptr(k), _ptr(v),
-        int(dst_rows), _ptr(dst_row), _ptr(dst_table), _ptr(dev_err), _stream(stream)))
-
-
 def pfd_decode_quant_workspace(batch, cu_lq_host, cu_k_host, Hq, Hkv, D, max_chunk_len, self_keys,
                                n_splits):
     a, b = _host_i32(cu_lq_host), _host_i32(cu_k_host)
     return load().pfd_decode_quant_workspace(batch, ctypes.cast(a, _P), ctypes.cast(b, _P), Hq, Hkv,
                                              D, max_chunk_len, int(self_keys), n_splits)
-
-
-def pfd_decode_attention_quant(q, k_self, v_self, cu_lq, cu_lq_host, format, pool_k, pool_v, exp_k,
-                               exp_v, pool_rows, table, table_len, sel, cu_k, cu_k_host, batch, Hq,
-                               Hkv, D, max_chunk_len, sm_scale, n_splits, out, lse, dev_err,
-                               workspace, workspace_bytes, stream=None):
-    a, b = _host_i32(cu_lq_host), _host_i32(cu_k_host)
-    _check(load().pfd_decode_attention_quant(
-        _ptr(q), _ptr(k_self), _ptr(v_self), _ptr(cu_lq), ctypes.addressof(a), format,
-        _ptr(pool_k), _ptr(pool_v), _ptr(exp_k), _ptr(exp_v), int(pool_rows), _ptr(table),
-        int(table_len), _ptr(sel), _ptr(cu_k), ctypes.addressof(b), batch, Hq, Hkv, D,
-        max_chunk_len, float(sm_scale), n_splits, _ptr(out), _ptr(lse), _ptr(dev_err),
-        _ptr(workspace), int(workspace_bytes), _stream(stream)))
-
-
-def pfd_decode_partial_quant(q, k_self, v_self, cu_lq, cu_lq_host, format, pool_k, pool_v, exp_k,
-                             exp_v, pool_rows, table, table_len, sel, cu_k, cu_k_host, batch, Hq,
-                             Hkv, D, max_chunk_len, sm_scale, self_keys, n_splits, part_o,
-                             part_lse, dev_err, workspace, workspace_bytes, stream=None):
-    a, b = _host_i32(cu_lq_host), _host_i32(cu_k_host)
-    _check(load().pfd_decode_partial_quant(
-        _ptr(q), _ptr(k_self), _ptr(v_self), _ptr(cu_lq), ctypes.addressof(a), format,
-        _ptr(pool_k), _ptr(pool_v), _ptr(exp_k), _ptr(exp_v), int(pool_rows), _ptr(table),
-        int(table_len), _ptr(sel), _ptr(cu_k), ctypes.addressof(b), batch, Hq, Hkv, D,
-        max_chunk_len, float(sm_scale), int(self_keys), n_splits, _ptr(part_o), _ptr(part_lse),
-        _ptr(dev_err), _ptr(workspace), int(workspace_bytes), _stream(stream)))
-
-
-def pfd_chunk_mass_quant(q, cu_lq, cu_lq_host, format, pool_k, exp_k, pool_rows, table, table_len,
-                         cu_n_host, lse, batch, Hq, Hkv, D, sm_scale, mass, dev_err, workspace,
-                         workspace_bytes, stream=None):
-    a, b = _host_i32(cu_lq_host), _host_i32(cu_n_host)
-    _check(load().pfd_chunk_mass_quant(
-        _ptr(q), _ptr(cu_lq), ctypes.addressof(a), format, _ptr(pool_k), _ptr(exp_k),
-        int(pool_rows), _ptr(table), int(table_len), ctypes.addressof(b), _ptr(lse), batch, Hq, Hkv,
-        D, float(sm_scale), _ptr(mass), _ptr(dev_err), _ptr(workspace), int(workspace_bytes),
-        _stream(stream)))

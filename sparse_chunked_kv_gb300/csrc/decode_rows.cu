@@ -152,19 +152,14 @@ constexpr int kStages = (192 * 1024) / (kWarps * Ring<D>::kBytes);
 
 template <int N>
 __device__ __forceinline__ void load_words(uint32_t (&w)[N], const uint8_t* src, bool ok) {
-  if constexpr (N == 2) {
-    const uint2 x = ok ? __ldg(reinterpret_cast<const uint2*>(src)) : make_uint2(0u, 0u);
-    w[0] = x.x;
-    w[1] = x.y;
-  } else {
+  static_assert(N % 4 == 0, "16-byte loads");
 #pragma unroll
-    for (int i = 0; i < N / 4; ++i) {
-      const uint4 x = ok ? __ldg(reinterpret_cast<const uint4*>(src) + i) : make_uint4(0u, 0u, 0u, 0u);
-      w[4 * i] = x.x;
-      w[4 * i + 1] = x.y;
-      w[4 * i + 2] = x.z;
-      w[4 * i + 3] = x.w;
-    }
+  for (int i = 0; i < N / 4; ++i) {
+    const uint4 x = ok ? __ldg(reinterpret_cast<const uint4*>(src) + i) : make_uint4(0u, 0u, 0u, 0u);
+    w[4 * i] = x.x;
+    w[4 * i + 1] = x.y;
+    w[4 * i + 2] = x.z;
+    w[4 * i + 3] = x.w;
   }
 }
 

@@ -32,7 +32,7 @@ struct Slot {
   int err;   // PFD_DEVERR_* of a slot that is skipped, else 0
 };
 
-// align: rows of the code side start at multiples of 16.
+// Slot j of a call; a slot's rows on the code side start at a multiple of 16.
 template <bool kToCodes>
 __device__ __forceinline__ Slot load_slot(const QuantParams& p, int j) {
   Slot s{0, 0, 0, 0};
