@@ -378,14 +378,24 @@ struct QuantPlan {
 
 // Whether a step over an 8-bit pool reads the selected chunks back to bf16 first.
 // The attention kernel converts a tile of 128 keys anew for every pair of
-// query tiles, which costs its softmax 0.8 us (the converters take issue slots);
-// staging costs a launch and the copy's traffic.  28 / 4 heads, D = 128, E4M3, in
-// kernel / staged: 16 sequences of 4112 keys, 54 tokens 90.5 / 104.1 us, 100
-// tokens 157.6 / 162.1, 144 tokens 179.1 / 172.9, 320 tokens 360.6 / 312.0; one of
-// 16448 keys, 144 tokens 50.8 / 52.7, 200 tokens 67.7 / 64.8, 320 tokens 97.0 /
-// 88.0; one of 1028 keys, 320 tokens 20.8 / 22.4.  A copy of more than 8 GB (the largest measured has 0.27)
-// is left out: max_chunk_len may be a loose bound, and nobody expects that
-// much workspace of a step.
+// query tiles, which costs its softmax 0.7 us (0.55 at D = 64; the converters take
+// issue slots); staging costs a launch and the copy's traffic.  In kernel / staged, us,
+// E4M3 and INT8, every chunk 257 rows:
+//   28 / 4 heads, D = 128, 16 x 16 chunks:
+//     54 tokens   90.6 / 104.6,  92.4 / 101.8    108 tokens 164.1 / 168.0, 167.0 / 165.9
+//     144 tokens 180.2 / 173.8, 183.1 / 171.0    324 tokens 363.9 / 314.6, 371.3 / 312.2
+//   28 / 4 heads, D = 64, 16 x 16 chunks:
+//     54 tokens   78.6 /  80.7,  75.2 /  80.4    108 tokens 131.3 / 130.6, 134.7 / 130.5
+//     216 tokens 217.7 / 200.8, 223.6 / 200.9    504 tokens 449.0 / 394.5, 464.4 / 394.7
+//   8 / 2 heads, D = 64, 64 chunks:
+//     256 tokens  29.2 /  30.0,  28.8 /  29.9    576 tokens  46.7 /  44.1,  46.7 /  44.0
+//   16 / 16 heads, D = 64, 64 chunks:
+//     384 tokens  86.0 /  87.4,  80.9 /  87.1    1024 tokens 151.8 / 148.5, 156.6 / 147.9
+//   32 / 8 heads, D = 128, 4 chunks:
+//     384 tokens  24.7 /  25.5,  24.9 /  25.5    896 tokens  42.1 /  38.3,  42.5 /  38.2
+// (over 112 shapes, each in both formats, the rule takes 0.1 % more than the better way
+// on average, 5 % at most).  A copy of more than 8 GB (the largest measured has 0.27) is left out: max_chunk_len may be a
+// loose bound, and nobody expects that much workspace of a step.
 bool stage_pays(int batch, const int32_t* cu_lq_host, const int32_t* cu_k_host, int Hq, int Hkv,
                 int D, int max_chunk_len) {
   const int Tq = kBlockM / (Hq / Hkv);
@@ -396,8 +406,8 @@ bool stage_pays(int batch, const int32_t* cu_lq_host, const int32_t* cu_k_host, 
     tiles += std::ceil(std::ceil(lq / Tq) / 2.0) * Hkv * (keys / kBlockN);
     values += keys * Hkv * D * 2.0;
   }
-  const double gain_us = 0.8 * tiles / device_sm_count();
-  const double cost_us = 5.0 + values * 3.0 / 7.3e6;
+  const double gain_us = (D == 64 ? 0.55 : 0.7) * tiles / device_sm_count();
+  const double cost_us = 3.0 + values * 3.0 / 7.3e6;
   return gain_us > cost_us && values * 2.0 <= 8e9;
 }
 

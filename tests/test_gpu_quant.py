@@ -536,7 +536,7 @@ MINUS_INF = {
     "rows": (5, [[64, 128]], 13),
     "tile": (30, [[64, 128]], 14),
     "tiles": (40, [[64, 128]], 15),
-    "staged": (320, [[2049] * 8], 64),
+    "staged": (352, [[2049] * 8], 64),
 }
 
 
@@ -598,6 +598,38 @@ def test_nan_shows_through_bf16_splits():
                                             table, st.sel, n_splits=n)
             assert torch.isnan(out[:, 4:]).all() and torch.isnan(lse[:, 4:]).all()
             assert torch.isfinite(out[:, :4]).all() and torch.isfinite(lse[:, :4]).all()
+
+
+def _assert_staged(st):
+    """The step's chunks are read back to bf16 first (its workspace holds the copy)."""
+    need = _abi.pfd_decode_quant_workspace(len(st.cu_lq) - 1, st.cu_lq, st.cu_k, st.hq, st.hkv, st.d,
+                                           st.max_len, int(st.self_keys), 1)
+    assert need >= st.cu_k[-1] * st.max_len * 4 * st.hkv * st.d
+
+
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("self_keys", [True, False])
+@pytest.mark.parametrize("d,lqs", [(64, [352, 65]), (128, [400, 65])])
+def test_staged_steps_match_the_reference(d, lqs, self_keys, fmt):
+    """Enough rows and keys that the chunks are read back first: a ragged batch."""
+    st = Step(fmt, 8, 2, d, lqs, [[2049] * 8, [300, 0, 2049, 1]], self_keys=self_keys, seed=44)
+    _assert_staged(st)
+    ref = st.reference()
+    for n_splits in (0, 1, 3, 64):
+        st.check(*st.run(n_splits), ref)
+
+
+@pytest.mark.parametrize("check", [
+    lambda: test_decode_bad_table_and_selection(352, 8),
+    lambda: test_decode_chunk_selected_twice(352, 8, "int8"),
+    lambda: test_decode_non_finite_live_rows(352, 8),
+    lambda: test_two_graphs_in_turn(352, 8),
+    lambda: test_scales_at_the_low_end("e4m3", 3, 352, 8)],
+    ids=["bad_entries", "twice", "non_finite", "graphs", "low_end"])
+def test_staged_steps_at_the_edges(check):
+    _assert_staged(Step("int8", 8, 2, 64, [352], [[64, 40, 17] + [2049] * 8]))
+    _assert_staged(Step("int8", 8, 2, 64, [352], [[64, 40] + [2049] * 8]))
+    check()
 
 
 def test_steps_without_rows_or_chunks():

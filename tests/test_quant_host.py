@@ -191,6 +191,22 @@ def test_workspace_of_a_loose_bound():
     assert need(1 << 20) == 0 and need(2 ** 31 - 1) == 0
 
 
+@pytest.mark.parametrize("hq,hkv,d,batch,chunks,rows,lq,staged", [
+    (28, 4, 128, 16, 16, 257, 108, False), (28, 4, 128, 16, 16, 257, 144, True),
+    (28, 4, 64, 16, 16, 257, 54, False), (28, 4, 64, 16, 16, 257, 144, True),
+    (8, 2, 64, 1, 64, 257, 256, False), (8, 2, 64, 1, 64, 257, 576, True),
+    (16, 16, 64, 1, 64, 257, 384, False), (16, 16, 64, 16, 16, 257, 384, True),
+    (32, 8, 128, 1, 4, 257, 384, False), (32, 8, 128, 1, 4, 257, 896, True),
+    (28, 4, 128, 1, 4, 257, 320, False), (28, 4, 128, 8, 8, 257, 320, True)])
+def test_when_chunks_are_read_back_first(hq, hkv, d, batch, chunks, rows, lq, staged):
+    """The faster of the two measured ways (the comment at stage_pays has the times),
+    by the workspace that a step of one split needs: the copy of its chunks, or none."""
+    need = _abi.pfd_decode_quant_workspace(batch, [lq * b for b in range(batch + 1)],
+                                           [chunks * b for b in range(batch + 1)], hq, hkv, d, rows, 1, 1)
+    copy = batch * chunks * rows * hkv * d * 4
+    assert copy <= need < copy + (1 << 16) if staged else need == 0
+
+
 # --------------------------------------------------------------- Python --
 
 def _no_library(monkeypatch):
