@@ -411,6 +411,29 @@ bool stage_pays(int batch, const int32_t* cu_lq_host, const int32_t* cu_k_host, 
   return gain_us > cost_us && values * 2.0 <= 8e9;
 }
 
+// Whether a step over an 8-bit pool runs by the few-rows kernel: up to 16 packed rows
+// always, 17 to 32 (four tiles of 8: a key group costs it 1.5 times as much as two
+// tiles do, and the start and the join of a CTA 4 us more at D = 128) where the steady
+// reading of a long cache pays for that.  groups: 16-key groups over all sequences and KV
+// heads.  Few-rows kernel / attention kernel, us, E4M3, by groups on each SM:
+//   D = 128:  1.8  (8 / 2 heads, 8 chunks of 257)       16 rows 11.1 / 10.0   32 rows 15.6 / 10.0
+//             7.2  (32 / 8 heads, 8 chunks of 257)      16 rows 11.4 / 11.0   32 rows 16.0 / 11.3
+//             28.6 (28 / 4 heads, 64 chunks of 257)     14 rows 13.3 / 17.3   28 rows 18.5 / 17.4
+//             54.3 (8 / 2 heads, 32 chunks of 2049)     16 rows 17.4 / 24.6   32 rows 25.5 / 24.8
+//             57.3 (8 / 2 heads, 16 x 16 of 257)        16 rows 17.8 / 25.8   32 rows 25.6 / 25.9
+//             114  (28 / 4 heads, 16 x 16 of 257)       14 rows 23.4 / 40.9   28 rows 35.1 / 40.8
+//             217  (32 / 8 heads, 32 chunks of 2049)    16 rows 34.4 / 58.1   32 rows 50.9 / 58.7
+//   D = 64:   3.6  (28 / 4 heads, 8 chunks of 257)      14 rows  9.1 /  9.1   28 rows 11.7 /  9.7
+//             14.3 (8 / 2 heads, 64 chunks of 257)      16 rows 10.7 / 13.5   32 rows 13.7 / 13.8
+//             27.8 (28 / 4 heads, 4 x 8 of 513)         14 rows 10.8 / 14.6   28 rows 14.2 / 14.9
+//             114  (28 / 4 heads, 16 x 16 of 257)       14 rows 18.6 / 38.1   28 rows 24.3 / 38.2
+// INT8 has the same crossings.  (One or two tiles, 4 to 16 rows, lose 10 % at most, at 2 to
+// 7 groups an SM and D = 128.)
+bool few_rows_pays(long long rows, long long groups, int D) {
+  if (rows <= kRowsMax / 2) return true;
+  return rows <= kRowsMax && groups >= (D == 64 ? 14LL : 55LL) * device_sm_count();
+}
+
 // Keys are counted in groups of 16, by the chunks' upper bound.  Every sequence is
 // split into items of at most the same share of groups; the share is the one
 // with the least expected time, in units of about a microsecond, of items that
@@ -431,25 +454,31 @@ QuantPlan plan_quant_decode(int batch, const int32_t* cu_lq_host, const int32_t*
   if (!decode_host_ok(batch, cu_lq_host, cu_k_host) || !shapes_ok(Hq, Hkv, 128)) return plan;
   const int G = Hq / Hkv;
   if (G > kBlockM) return plan;
-  long long lq_max = 0;
-  for (int b = 0; b < batch; ++b)
+  const long long chunk_groups = (std::max(0, max_chunk_len) + kGroupRows - 1LL) / kGroupRows;
+  auto groups_of = [&](int b) {
+    const long long lq = cu_lq_host[b + 1] - cu_lq_host[b];
+    return lq == 0 ? 0LL
+                   : (cu_k_host[b + 1] - cu_k_host[b]) * chunk_groups +
+                         (self_keys ? (lq + kGroupRows - 1) / kGroupRows : 0);
+  };
+  long long lq_max = 0, groups_sum = 0;
+  for (int b = 0; b < batch; ++b) {
     lq_max = std::max<long long>(lq_max, cu_lq_host[b + 1] - cu_lq_host[b]);
-  plan.rows = lq_max * G <= kRowsMax;
+    groups_sum += groups_of(b);
+  }
+  plan.rows = few_rows_pays(lq_max * G, groups_sum * Hkv, D);
   plan.row_tiles = lq_max * G <= 8 ? 1 : lq_max * G <= 16 ? 2 : 4;
   plan.staged = !plan.rows && stage_pays(batch, cu_lq_host, cu_k_host, Hq, Hkv, D, max_chunk_len);
   // Groups and items (of one split and head) of each sequence.
   const bool listed = batch <= kMaxSeqItems;
   const int pair_tokens = 2 * (kBlockM / G);
-  const long long chunk_groups = (std::max(0, max_chunk_len) + kGroupRows - 1LL) / kGroupRows;
   auto pairs_of = [&](long long lq) {
     return plan.rows ? (lq > 0 ? 1LL : 0LL) : (lq + pair_tokens - 1) / pair_tokens;
   };
   long long groups[kMaxSeqItems], pairs[kMaxSeqItems], groups_max = 1;
   for (int b = 0; b < batch; ++b) {
     const long long lq = cu_lq_host[b + 1] - cu_lq_host[b];
-    const long long g = lq == 0 ? 0
-                                : (cu_k_host[b + 1] - cu_k_host[b]) * chunk_groups +
-                                      (self_keys ? (lq + kGroupRows - 1) / kGroupRows : 0);
+    const long long g = groups_of(b);
     groups_max = std::max(groups_max, g);
     if (listed) {
       groups[b] = g;

@@ -600,6 +600,51 @@ def test_nan_shows_through_bf16_splits():
             assert torch.isfinite(out[:, :4]).all() and torch.isfinite(lse[:, :4]).all()
 
 
+@pytest.mark.parametrize("fmt", FORMATS)
+@pytest.mark.parametrize("self_keys", [True, False])
+@pytest.mark.parametrize("hq,hkv,d,lqs,chunk_lens", [
+    (16, 16, 64, [32], [[2049, 129]]), (16, 16, 64, [17, 3, 20], [[900], [], [2049, 0, 16, 200]]),
+    (28, 4, 64, [4], [[2049] * 4 + [513]]), (16, 16, 128, [20], [[2049] * 4 + [129]]),
+    (64, 16, 128, [8, 1], [[2049] * 4, [130, 7]])])
+def test_long_steps_of_17_to_32_rows(hq, hkv, d, lqs, chunk_lens, self_keys, fmt):
+    """So many keys that the few-rows kernel takes them, with four tiles of rows."""
+    st = Step(fmt, hq, hkv, d, lqs, chunk_lens, self_keys=self_keys, seed=45)
+    groups = sum(-(-st.max_len // 16) * len(c) for c in chunk_lens) * hkv
+    assert groups >= (14 if d == 64 else 55) * torch.cuda.get_device_properties(0).multi_processor_count
+    ref = st.reference()
+    for n_splits in (0, 1, 3, 64):
+        st.check(*st.run(n_splits), ref)
+    again, lse = st.run(3)
+    st.check(again, lse, ref)
+
+
+@pytest.mark.parametrize("lq", [17, 32])
+def test_long_steps_of_17_to_32_rows_at_the_edges(lq):
+    """Rising logits, and live keys at -inf, NaN and infinity."""
+    st = Step("e4m3", 16, 16, 64, [lq], [[128] * 18], seed=46)
+    st.q = st.q.abs()
+    st.pool.k.view(torch.uint8).bitwise_and_(0x7F)
+    st.pool.k.view(torch.uint8)[st.pool.k.view(torch.uint8) == 0x7F] = 0
+    for j, c in enumerate(st.sel_host):
+        row = int(st.table[c, 0].item()) // 16
+        st.pool.exp_k[row:row + 8] += max(0, (j - 8) // 2)
+    st.k_self[:, :, 7] = -math.inf
+    st.q[:, :, 7] += 0.5
+    host = st.table.cpu().numpy()
+    keys, vals = (R.keys_of(values_of(st.pool, x), host, st.sel_host) for x in "kv")
+    ref = R.decode(f64(st.q), keys, vals, 1 / 8)
+    for n in (1, 2, 64):
+        st.check(*st.run(n), ref)
+    st.k_self = draw_rows("normal", lq, 16, 64, 1)
+    clean = st.reference()
+    st.q[1, 3, 9] = math.nan
+    for n in (1, 3):
+        out, lse = (x.cpu() for x in st.run(n))
+        assert torch.isnan(out[1, 3]).all() and torch.isnan(lse[1, 3])
+        out[1, 3], lse[1, 3] = torch.from_numpy(clean[0][1, 3]).to(out.dtype), float(clean[1][1, 3])
+        st.check(out, lse, clean)
+
+
 def _assert_staged(st):
     """The step's chunks are read back to bf16 first (its workspace holds the copy)."""
     need = _abi.pfd_decode_quant_workspace(len(st.cu_lq) - 1, st.cu_lq, st.cu_k, st.hq, st.hkv, st.d,

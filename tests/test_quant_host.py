@@ -207,6 +207,25 @@ def test_when_chunks_are_read_back_first(hq, hkv, d, batch, chunks, rows, lq, st
     assert copy <= need < copy + (1 << 16) if staged else need == 0
 
 
+@pytest.mark.parametrize("hq,hkv,d,batch,chunks,rows,few", [
+    (8, 2, 128, 1, 8, 257, False), (8, 2, 128, 1, 100, 513, False), (8, 2, 128, 2, 64, 513, True),
+    (8, 2, 128, 1, 64, 2049, True), (8, 2, 64, 1, 8, 257, False), (8, 2, 64, 1, 100, 513, True),
+    (32, 8, 128, 1, 8, 257, False), (32, 8, 128, 4, 64, 513, True), (32, 8, 64, 4, 64, 513, True)])
+def test_which_kernel_takes_17_to_32_rows(hq, hkv, d, batch, chunks, rows, few):
+    """The faster of the two measured (the comment at few_rows_pays has the times).
+    Each has a plan of its own for the splits: 32 rows are split as 16 are where the
+    few-rows kernel takes them, else as 36 are."""
+    def splits(lq):
+        need = _abi.pfd_decode_quant_workspace(batch, [lq * b for b in range(batch + 1)],
+                                               [chunks * b for b in range(batch + 1)], hq, hkv, d,
+                                               rows, 1, 0)
+        return need // (batch * lq * hq * (8 + 4 * d))
+    assert hq // hkv == 4
+    one, two = splits(4), splits(9)
+    assert one != two
+    assert splits(8) == (one if few else two)
+
+
 # --------------------------------------------------------------- Python --
 
 def _no_library(monkeypatch):
