@@ -264,9 +264,9 @@ struct Join {
 // The rings, and after the last group the warps' outputs.
 template <int D, int NT>
 constexpr int rows_smem_bytes() {
-  const int ring = kWarps * kStages<D> * Ring<D>::kBytes;
+  const int ring = 1024 + kWarps * kStages<D> * Ring<D>::kBytes;
   const int join = kWarps * 8 * NT * Join<D>::kPitch * 4;
-  return 1024 + (ring > join ? ring : join);   // (the start's alignment)
+  return ring > join ? ring : join;
 }
 
 // kSeqItems: items by sequence, of a ragged batch.
@@ -277,7 +277,7 @@ decode_rows_kernel(const __grid_constant__ RowsParams p) {
   constexpr int kRows = 8 * NT;
   constexpr int kStages = pfd::kStages<D>;
   constexpr int kPad = 8;
-  extern __shared__ uint8_t smem_raw[];
+  extern __shared__ __align__(16) float o_sm[];   // rings; then the warps' outputs [warp][row][column]
   __shared__ uint64_t full[kWarps][kStages];
   __shared__ int32_t seg_row[kMaxSegments], seg_len[kMaxSegments], seg_g0[kMaxSegments + 1];
   __shared__ float sm_m[kWarps][kRows], sm_y[kWarps][kRows], sm_l[kWarps][kRows];
@@ -390,11 +390,8 @@ decode_rows_kernel(const __grid_constant__ RowsParams p) {
     }
     return x;
   };
-  // The rings begin at 1024 bytes (TMA's swizzle); where they were, the warps'
-  // outputs [warp][row][column] follow, in 16-byte accesses.
   uint8_t* const rings =
-      reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~static_cast<uintptr_t>(1023));
-  float* const o_sm = reinterpret_cast<float*>(rings);
+      reinterpret_cast<uint8_t*>((reinterpret_cast<uintptr_t>(o_sm) + 1023) & ~static_cast<uintptr_t>(1023));
   uint8_t* const ring = rings + warp * (kStages * R::kBytes);
   int base = 0;   // the lanes hold the places of pairs base .. base + 31
   Place here = look_up(base);
