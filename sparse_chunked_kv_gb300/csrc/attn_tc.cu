@@ -1042,7 +1042,7 @@ attention_kernel(const __grid_constant__ AttnParams p) {
         // Mass items: every probability is taken at the step's normaliser,
         // p = 2^(s * scale - lse * log2(e)), so the row's reference is its
         // lse and never moves (rows past the block, or with no finite lse,
-        // get +inf: their probabilities are 0).
+        // get +inf, by which the epilogue leaves them out).
         const int t_local = row / G;
         const int t = (it.ta + x) * p.Tq + t_local;
         float b = INFINITY;

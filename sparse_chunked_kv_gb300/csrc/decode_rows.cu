@@ -33,10 +33,12 @@
 //     group of 16.
 // The warps' states (m, y, l, O) are joined in shared memory in a fixed order,
 // the splits' states by the merge kernel.
-// 28 / 4 heads, D = 128: 1 token over 131,136 rows 30.7 us with the merge (4.4 TB/s;
-// 81 by the attention kernel; 55 with 16-row tiles loaded straight to registers, 35.8
-// with the rings), 28 rows over 16 x 4112 keys 33.6 us (41 by the attention kernel, which
-// takes over past 32 rows: 63 rows 59.6 / 41).
+// 28 / 4 heads, D = 128: 1 token over 131,136 rows 30.9 us with the merge (4.3 TB/s;
+// 55 with 16-row tiles loaded straight to registers, 35.8 with the rings); over 65,568 rows
+// 16.6 us, 33.4 by the attention kernel, 4 tokens (28 rows) 30.2 and 33.7.  Which of the
+// two takes 17 to 32 rows: few_rows_pays in pfd_api.cu.  (The join of
+// 64 rows' outputs would not fit in shared memory.  At D = 128 the 32-row instances are at
+// 255 registers and spill 136 to 148 bytes.)
 #include "pfd_internal.cuh"
 #include "sm103_ptx.cuh"
 
