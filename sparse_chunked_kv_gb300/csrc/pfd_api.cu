@@ -394,8 +394,9 @@ struct QuantPlan {
 //   32 / 8 heads, D = 128, 4 chunks:
 //     384 tokens  24.7 /  25.5,  24.9 /  25.5    896 tokens  42.1 /  38.3,  42.5 /  38.2
 // (over 112 shapes, each in both formats, the rule takes 0.1 % more than the better way
-// on average, 5 % at most).  A copy of more than 8 GB (the largest measured has 0.27) is left out: max_chunk_len may be a
-// loose bound, and nobody expects that much workspace of a step.
+// on average, 5 % at most).  A copy of more than 8 GB (the largest measured has 0.27) is
+// left out: max_chunk_len may be a loose bound, and nobody expects that much workspace of
+// a step.
 bool stage_pays(int batch, const int32_t* cu_lq_host, const int32_t* cu_k_host, int Hq, int Hkv,
                 int D, int max_chunk_len) {
   const int Tq = kBlockM / (Hq / Hkv);

@@ -53,7 +53,7 @@ def _rows(tensor, what):
 
 def _apart(written, what, **read):
     """The entries that a call writes share no memory with those it reads."""
-    if written is None:
+    if written is None or written.numel() == 0:
         return
     start = written.data_ptr()
     end = start + written.numel() * written.element_size()

@@ -74,6 +74,12 @@ def test_the_written_table_is_apart_from_what_is_read(lib, name, args, written, 
             assert _call(lib, name, args, over) == INVALID, (other, at)
 
 
+def test_no_entries_share_nothing():
+    t = _i32(8, 2)
+    quant._apart(t[3:3], "dst_table", table=t)
+    quant._apart(t[3:5], "dst_table", table=t[4:4], sel=t[:3].view(-1), dst_row=None)
+
+
 def test_shared_entries_are_refused(monkeypatch):
     monkeypatch.setattr(quant, "_need", lambda *a: None)
     _no_library(monkeypatch)
