@@ -8,7 +8,10 @@ KV head; slots start at multiples of 16 rows.
 
 Every call runs on the device of its tensors, on that device's current stream
 or on `stream` (a torch stream, or a raw cudaStream_t).  What a call allocates
-(outputs that were not passed, workspace) belongs to the stream it runs on.
+(outputs that were not passed, workspace) belongs to the stream it runs on, and
+what it is given is marked as in use there (Tensor.record_stream), so that a
+temporary of another stream may be dropped at once; ordering the streams is the
+caller's.
 The calls neither copy between host and device nor wait, once a plan is made
 and max_len is given, so they may be captured into a CUDA graph.
 """
@@ -70,7 +73,7 @@ def _error_word(dev_err, device):
 
 
 @contextlib.contextmanager
-def _switched(device, stream):
+def _switched(device, stream, given):
     with torch.cuda.device(device):
         if stream is None:
             yield
@@ -78,18 +81,23 @@ def _switched(device, stream):
             if isinstance(stream, int):
                 stream = (torch.cuda.ExternalStream(stream, device=device) if stream
                           else torch.cuda.default_stream(device))
+            if stream != torch.cuda.current_stream(device):
+                for t in given:
+                    if t is not None:
+                        t.record_stream(stream)
             with torch.cuda.stream(stream):
                 yield
 
 
-def _call(device, stream, body):
-    """Runs body() with the call's device and stream the current ones."""
+def _call(device, stream, body, given):
+    """Runs body() with the call's device and stream the current ones; given():
+    the tensors it uses."""
     if stream is None:
         if device.index == torch.cuda.current_device():
             return body()
     elif not isinstance(stream, int) and stream.device != device:
         raise ValueError(f"stream: on {stream.device}, the call on {device}")
-    with _switched(device, stream):
+    with _switched(device, stream, given() if stream is not None else ()):
         return body()
 
 
@@ -119,20 +127,20 @@ class QuantPool:
         _need(v, k.dtype, k.shape, "pool v", k.device)
         _need(exp_k, _U8, exps, "pool exp_k", k.device)
         _need(exp_v, _U8, exps, "pool exp_v", k.device)
-        self._tensors = (k, v, exp_k, exp_v)
+        self.tensors = (k, v, exp_k, exp_v)
         self.rows, self.n_kv_heads, self.head_dim = rows, hkv, d
         self.device, self.format = k.device, _FORMATS[k.dtype]
 
     # Read-only: their types and shapes are checked once, when the pool is made.
-    k = property(lambda self: self._tensors[0])
-    v = property(lambda self: self._tensors[1])
-    exp_k = property(lambda self: self._tensors[2])
-    exp_v = property(lambda self: self._tensors[3])
+    k = property(lambda self: self.tensors[0])
+    v = property(lambda self: self.tensors[1])
+    exp_k = property(lambda self: self.tensors[2])
+    exp_v = property(lambda self: self.tensors[3])
 
     @property
     def pointers(self):
         """Addresses of k, v, exp_k and exp_v now."""
-        k, v, exp_k, exp_v = self._tensors
+        k, v, exp_k, exp_v = self.tensors
         return k.data_ptr(), v.data_ptr(), exp_k.data_ptr(), exp_v.data_ptr()
 
     @classmethod
@@ -168,6 +176,7 @@ class _Plan:
         self.cu_chunks_host = (ctypes.c_int32 * len(cu_chunks))(*cu_chunks)
         self.cu_lq = torch.tensor(cu_lq, dtype=torch.int32, device=self.device)
         self.cu_chunks = torch.tensor(cu_chunks, dtype=torch.int32, device=self.device)
+        self.tensors = (self.cu_lq, self.cu_chunks)
         self.pointers = (self.cu_lq.data_ptr(), ctypes.addressof(self.cu_lq_host),
                          self.cu_chunks.data_ptr(), ctypes.addressof(self.cu_chunks_host))
         self.kv_shape = (self.total_lq, n_kv_heads, head_dim)
@@ -251,7 +260,8 @@ def pool_quantize(k, v, src_table, pool, slot_row, max_len=None, table=None, dev
                 slot_row.data_ptr(), out.data_ptr(), err, _raw_stream(dev)))
         return out
 
-    return _call(dev, stream, body)
+    return _call(dev, stream, body,
+                 lambda: (k, v, src_table, *pool.tensors, slot_row, table, dev_err))
 
 
 def pool_dequantize(pool, table, dst_row, dst_rows=None, sel=None, max_len=None, k=None, v=None,
@@ -296,7 +306,8 @@ def pool_dequantize(pool, table, dst_row, dst_rows=None, sel=None, max_len=None,
                 to_table.data_ptr(), err, _raw_stream(dev)))
         return to_k, to_v, to_table
 
-    return _call(dev, stream, body)
+    return _call(dev, stream, body,
+                 lambda: (*pool.tensors, table, dst_row, sel, k, v, dst_table, dev_err))
 
 
 def _check_step(q, pool, plan, lse):
@@ -341,7 +352,8 @@ def _decode(name, q, k_self, v_self, pool, table, sel, plan, extra, out, lse, de
             None if ws is None else ws.data_ptr(), plan.workspace_bytes, _raw_stream(dev)))
         return to, to_lse
 
-    return _call(dev, stream, body)
+    return _call(dev, stream, body, lambda: (q, k_self, v_self, *pool.tensors, table, sel, *plan.tensors,
+                                             out, lse, dev_err, space))
 
 
 def decode_attention_quant(q, k_self, v_self, pool, table, sel, plan, out=None, lse=None,
@@ -394,4 +406,5 @@ def chunk_mass_quant(q, pool, table, lse, plan, mass=None, dev_err=None, workspa
             None if ws is None else ws.data_ptr(), plan.workspace_bytes, _raw_stream(dev)))
         return to
 
-    return _call(dev, stream, body)
+    return _call(dev, stream, body, lambda: (q, pool.k, pool.exp_k, table, lse, *plan.tensors, mass,
+                                             dev_err, space))

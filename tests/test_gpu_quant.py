@@ -967,6 +967,46 @@ def test_two_streams_at_once():
         assert torch.equal(out, want[0]) and torch.equal(lse, want[1])
 
 
+@pytest.mark.parametrize("raw", [False, True])
+@pytest.mark.parametrize("lq", [1, 40])
+def test_temporaries_of_another_stream(lq, raw):
+    """What a call is given may be dropped when it returns, although the call runs
+    later, on a stream that is still busy: its memory is not handed out again before."""
+    st = Step("e4m3", 8, 2, 64, [lq], [[64, 40, 17]], seed=47)
+    n = st.table.shape[0]
+    plan = api.QuantDecodePlan(st.cu_lq, st.cu_k, 8, 2, 64, st.max_len)
+    mplan = api.QuantMassPlan(st.cu_lq, [0, n], 8, 2, 64)
+    q, k, v = P.cuda(st.q), P.cuda(st.k_self), P.cuda(st.v_self)
+    x, y = P.cuda(draw_rows("normal", 48, 2, 64, 1)), P.cuda(draw_rows("normal", 48, 2, 64, 2))
+    want = api.decode_attention_quant(q, k, v, st.pool, st.table, st.sel, plan)
+    want_mass = api.chunk_mass_quant(q, st.pool, st.table, want[1], mplan)
+    pools = [api.QuantPool.zeros(48, 2, 64) for _ in range(2)]
+    api.pool_quantize(x, y, ints([[0, 48]]), pools[0], ints([0]), max_len=48)
+    back = api.pool_dequantize(st.pool, st.table, st.table[:, 0].contiguous(), st.pool.rows,
+                               max_len=st.max_len)
+    side = torch.cuda.Stream()
+    at = side.cuda_stream if raw else side
+    torch.cuda.synchronize()
+    with torch.cuda.stream(side):
+        torch.cuda._sleep(100_000_000)   # about 50 ms
+    got = api.decode_attention_quant(q.clone(), k.clone(), v.clone(), st.pool, st.table.clone(),
+                                     st.sel.clone(), plan, stream=at)
+    mass = api.chunk_mass_quant(q.clone(), st.pool, st.table.clone(), want[1].clone(), mplan, stream=at)
+    api.pool_quantize(x.clone(), y.clone(), ints([[0, 48]]), pools[1], ints([0]), max_len=48, stream=at)
+    rows = api.pool_dequantize(st.pool, st.table.clone(), st.table[:, 0].clone(), st.pool.rows,
+                               max_len=st.max_len, stream=at)
+    # takes whatever the temporaries have left
+    over = [torch.full_like(t, 1) for t in (q, k, v, st.table, st.sel, want[1], x, y) for _ in range(8)]
+    torch.cuda.synchronize()
+    assert len(over) == 64
+    assert torch.equal(got[0], want[0]) and torch.equal(got[1], want[1]) and torch.equal(mass, want_mass)
+    for a, b in zip(pools[0].tensors, pools[1].tensors):
+        assert torch.equal(a.view(torch.uint8), b.view(torch.uint8))
+    for row, length in st.table.cpu().tolist():   # (what no slot covers is undefined)
+        for a, b in zip(rows[:2], back[:2]):
+            assert torch.equal(a[row:row + length], b[row:row + length])
+
+
 def test_pool_past_four_gigabytes():
     """Rows past 2^32 bytes of codes are written and read at their place."""
     hkv, d = 8, 128

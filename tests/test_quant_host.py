@@ -244,11 +244,13 @@ class _Pool:
     """A pool's outline on the host (QuantPool itself takes CUDA tensors only)."""
     device, n_kv_heads, head_dim, rows, format = torch.device("cuda", 0), 2, 64, 32, 0
     k = v = exp_k = exp_v = None
+    tensors = ()
 
 
 class _Plan:
     device, n_kv_heads, n_q_heads, head_dim = torch.device("cuda", 0), 2, 4, 64
     total_lq, total_chunks, self_keys, complete = 3, 1, True, True
+    tensors = ()
 
 
 def _bf(*shape):
