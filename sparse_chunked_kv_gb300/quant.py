@@ -13,7 +13,8 @@ what it is given is marked as in use there (Tensor.record_stream), so that a
 temporary of another stream may be dropped at once; ordering the streams is the
 caller's.
 The calls neither copy between host and device nor wait, once a plan is made
-and max_len is given, so they may be captured into a CUDA graph.
+and max_len is given, so they may be captured into a CUDA graph.  The graph keeps
+addresses: the plan, the pool and the tensors given have to live as long as it.
 """
 from __future__ import annotations
 
